@@ -535,7 +535,8 @@ fa_status fa_pages_compact(void* const* pools, const size_t* page_bytes, int n_p
  *                 cu_batch[g+1]-1.  NULL with G = 1: the whole batch.  Entries
  *                 of no group have no prefix.  A group that runs backwards or
  *                 leaves the batch is taken as empty and FA_ERR_INVALID_ARG is
- *                 recorded in the device error word.
+ *                 recorded in the device error word; a group behind it begins no
+ *                 earlier than the largest end of the groups before it.
  *   block_table : int32 [B, pages_per_seq], row stride table_stride, and
  *   seqlens     : int32 [B], device: each sequence's own pages and length
  *                 (not counting the prefix).

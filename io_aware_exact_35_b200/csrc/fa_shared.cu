@@ -112,16 +112,42 @@ struct Params {
   float scale_log2;
 };
 
-// First and last batch entry of group g.  A group that leaves the batch or
-// runs backwards is empty and reported.
-__device__ __forceinline__ void group_range(const int* cu, int B, int g, int& b0, int& b1) {
-  b0 = cu == nullptr ? 0 : cu[g];
-  b1 = cu == nullptr ? B : cu[g + 1];
-  if (b0 < 0 || b1 < b0 || b1 > B) {
-    record_error(1 /* FA_ERR_INVALID_ARG */);
+// One warp: first and last batch entry of the groups, 32 at a time in their order
+// (g0 = 0, 32, ..; lane i takes group g0 + i).  A group that leaves the batch or
+// runs backwards is empty and reported.  Each group begins where the one before it
+// ends, so they are disjoint until one is refused; from then on a group begins no
+// earlier than the largest end so far.  An entry therefore has one group, whose CTAs
+// alone write its partials, and there are no more row tiles than the grid has.
+struct GroupRanges {
+  int end = 0;        // the largest end of the groups before g0
+  bool chain = true;  // none of them was refused
+  __device__ __forceinline__ void take(const int* cu, int B, int G, int g0, int& b0, int& b1) {
+    const int g = g0 + static_cast<int>(threadIdx.x & 31);
+    bool bad = false;
     b0 = b1 = 0;
+    if (g < G) {
+      b0 = cu == nullptr ? 0 : cu[g];
+      b1 = cu == nullptr ? B : cu[g + 1];
+      bad = b0 < 0 || b1 < b0 || b1 > B;
+      if (bad) {
+        record_error(1 /* FA_ERR_INVALID_ARG */);
+        b0 = b1 = 0;
+      }
+    }
+    const int most = __reduce_max_sync(0xffffffffu, b1);
+    chain = chain && !__any_sync(0xffffffffu, bad);
+    if (!chain) {
+      int upto = b1;  // the largest end up to this lane, then before it
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1)
+        upto = max(upto, __shfl_up_sync(0xffffffffu, upto, off));
+      const int before = __shfl_up_sync(0xffffffffu, upto, 1);
+      b0 = max(b0, max(end, (threadIdx.x & 31) == 0 ? 0 : before));
+      b1 = max(b0, b1);
+    }
+    end = max(end, most);
   }
-}
+};
 
 __device__ __forceinline__ int prefix_len(const int* lens, int g, int pages, int log2_page) {
   const long long cap = static_cast<long long>(pages) << log2_page;
@@ -212,11 +238,12 @@ __device__ __forceinline__ bool find_tile(const Params& p, int r, int tile, int 
                                           int& local, int& g, int& b0, int& b1, int& len) {
   const int lane = threadIdx.x & 31;
   int before = 0;
+  GroupRanges ranges;
   for (int g0 = 0; g0 < p.G; g0 += 32) {
-    int n = 0, first = 0, last = 0, length = 0;
+    int n = 0, first, last, length = 0;
+    ranges.take(p.cu, p.B, p.G, g0, first, last);
     if (g0 + lane < p.G) {
       length = prefix_len(p.lens, g0 + lane, p.pages, p.log2_page);
-      group_range(p.cu, p.B, g0 + lane, first, last);
       n = (static_cast<int>(static_cast<long long>(last - first) * r) + tile_rows - 1) / tile_rows;
     }
     int upto = n;
@@ -1164,14 +1191,14 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32)
     own = p.own_count[static_cast<size_t>(b) * p.Hkv * tiles + h / r * tiles + h % r / 16];
     own_keys = own_len(seqlens, b, Lmax);
   }
-  int group = -1, length = 0;  // the first that b belongs to
+  int group = -1, length = 0;  // the one that b belongs to
+  GroupRanges ranges;
   for (int g0 = 0; g0 < p.G && group < 0; g0 += 32) {
     bool mine = false;
-    int len = 0;
+    int len = 0, b0, b1;
+    ranges.take(p.cu, p.B, p.G, g0, b0, b1);
     if (g0 + lane < p.G) {
-      int b0, b1;
       len = prefix_len(p.lens, g0 + lane, p.pages, p.log2_page);
-      group_range(p.cu, p.B, g0 + lane, b0, b1);
       mine = b >= b0 && b < b1;
     }
     const unsigned m = __ballot_sync(0xffffffffu, mine);
