@@ -38,6 +38,7 @@
 // tokens x 32 heads, 403 MB, 75.6, 8.9K tokens into pages, 218 MB, 40.8.
 #include <type_traits>
 
+#include "fa_angle.h"
 #include "fa_internal.h"
 #include "sm100.cuh"
 
@@ -134,41 +135,6 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
   float a, b;
   f2_split(v, a, b);
   return a + b;
-}
-
-// x mod 1 in units of 2^-64, x >= 0.
-__device__ __forceinline__ unsigned long long fraction(double x) {
-  x -= floor(x);
-  const double hi = floor(x * 4294967296.0);  // two steps: a double holds 53 bits
-  const double lo = (x * 4294967296.0 - hi) * 4294967296.0;
-  return (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
-}
-// Turns per position: f / (2 pi).  1 / (2 pi) is taken as 29 bits, whose product
-// with the 24 bits of f is exact, and a remainder.
-__device__ __forceinline__ unsigned long long turns(float f) {
-  const double x = fabs(static_cast<double>(f));
-  const unsigned long long t = fraction(x * 0.15915494272485375) + fraction(x * 3.6704158172530464e-10);
-  return f < 0.f ? 0ull - t : t;
-}
-
-// cos and sin of position * frequency: the product's fraction of a turn, its
-// nearest quarter turn, and the Taylor series about it to the ninth and eighth
-// power (|theta| <= pi / 4: remainders 1.8e-9 and 2.5e-8).
-__device__ __forceinline__ void turn(int pos, unsigned long long f, float& c, float& s) {
-  const int frac = static_cast<int>((static_cast<unsigned long long>(static_cast<long long>(pos)) * f) >> 32);
-  const int quarter = (frac + (1 << 29)) >> 30;  // wraps: -2 .. 1, two of them the half turn
-  const float th = static_cast<float>(frac - static_cast<int>(static_cast<unsigned>(quarter) << 30)) *
-                   1.4629180792671596e-9f;       // 2 pi / 2^32
-  const float x = th * th;
-  const float si = fmaf(th * x, fmaf(x, fmaf(x, fmaf(x, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f),
-                                     -1.6666667e-1f), th);
-  const float co = fmaf(x, fmaf(x, fmaf(x, fmaf(x, 2.4801587e-5f, -1.3888889e-3f), 4.1666667e-2f), -0.5f),
-                        1.f);
-  const bool swap = (quarter & 1) != 0;
-  c = swap ? si : co;
-  s = swap ? co : si;
-  if (((quarter + 1) & 2) != 0) c = -c;          // quarters 1 and 2
-  if ((quarter & 2) != 0) s = -s;                // quarters 2 and 3
 }
 
 // Where a lane's eight pairs stand in the row.  Neighbouring lanes hold
@@ -737,7 +703,7 @@ fa_status launch_fwd(Params& p, cudaStream_t stream) {
   const int tokens = GROUPS / p.gpt;
   const int tiles = (p.T + tokens - 1) / tokens;
   const int grid = tiles < FWD_CTAS * sms ? tiles : FWD_CTAS * sms;
-  // at most 24 KB and 16 KB of angles, below the 48 KB that need no opt-in
+  // 16 KB of rows and at most 16 KB of angles, below the 48 KB that need no opt-in
   const int smem = Ahead<FWD_STAGES, 2>::BYTES + 2 * tokens * p.R * static_cast<int>(sizeof(float));
   fa_qk_norm_rope_kernel<D, INTER, FULL, APPEND><<<grid, THREADS, smem, stream>>>(p);
   return cuda_status(cudaGetLastError());
