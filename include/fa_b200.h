@@ -372,7 +372,8 @@ fa_status fa_decode_static(const void* q, const void* kcache, const void* vcache
  *   q_weight, k_weight : [d] bf16 or float32 (weight_type), or NULL.
  *   positions : int32, token n of batch b at b * pos_batch_stride + n (stride
  *               0: the same positions for every batch), on the device.
- *   inv_freq  : float32 [rotary_dim / 2], on the device.
+ *   inv_freq  : float32 [rotary_dim / 2], on the device.  One that is infinite
+ *               or NaN makes its pair NaN at every position.
  *   rotary_dim: 0 to d, a multiple of 16 (0: no rotation; positions and
  *               inv_freq may then be NULL).
  *   H, Hkv    : heads of q and of k; one of them may be 0.

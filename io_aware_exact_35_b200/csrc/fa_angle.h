@@ -24,11 +24,16 @@ FA_ANGLE_FN unsigned long long fraction(double x) {
   return (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
 }
 // Turns per position: f / (2 pi).  1 / (2 pi) is taken as 29 bits, whose product
-// with the 24 bits of f is exact, and a remainder.
+// with the 24 bits of f is exact, and a remainder.  A frequency that is no finite
+// number has no turn: it is NO_TURN, and the one finite fraction of that value (2^-64
+// of a turn, 2^-33 after 2^31 positions) is taken as none.
+constexpr unsigned long long NO_TURN = 1;
 FA_ANGLE_FN unsigned long long turns(float f) {
   const double x = fabs(static_cast<double>(f));
-  const unsigned long long t = fraction(x * 0.15915494272485375) + fraction(x * 3.6704158172530464e-10);
-  return f < 0.f ? 0ull - t : t;
+  if (!(x <= 3.5e38)) return NO_TURN;  // past the largest float: infinite, or NaN
+  unsigned long long t = fraction(x * 0.15915494272485375) + fraction(x * 3.6704158172530464e-10);
+  if (f < 0.f) t = 0ull - t;
+  return t == NO_TURN ? 0 : t;
 }
 
 // cos and sin of position * frequency: the product's fraction of a turn, its
@@ -51,6 +56,7 @@ FA_ANGLE_FN void turn(int pos, unsigned long long f, float& c, float& s) {
   s = swap ? co : si;
   if (((quarter + 1) & 2) != 0) c = -c;          // quarters 1 and 2
   if ((quarter & 2) != 0) s = -s;                // quarters 2 and 3
+  if (f == NO_TURN) c = s = NAN;
 }
 
 }  // namespace rope

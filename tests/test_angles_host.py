@@ -71,3 +71,22 @@ def test_far_positions(angles):
     freq[::5] *= -1
     freq[:3] = 0.0, 1.0, 2.0 ** -20
     _check(angles(pos, freq), pos, freq)
+
+
+def test_frequencies_that_are_no_finite_numbers(angles):
+    pos = np.array([0, 1, -7, 2 ** 31 - 1])
+    for f in (math.inf, -math.inf, math.nan):
+        assert np.isnan(angles(pos, np.full(4, f, dtype=np.float32))).all()
+
+
+def test_least_and_largest_frequencies(angles):
+    """Frequencies about the least fraction that is held (2^-64 of a turn is
+    3.4e-19), denormal and very large ones."""
+    tiny = np.array([3.3e-19, 3.5e-19, 5e-19, 6.7e-19, 7e-19, 1.4e-45, 1e-38], dtype=np.float32)
+    freq = np.concatenate((tiny, -tiny))
+    for p in (0, 1, -1, 2 ** 31 - 1, -2 ** 31):
+        pos = np.full(len(freq), p)
+        _check(angles(pos, freq), pos, freq)
+    big = np.array([3.4e38, 1e30, 2.0 ** 60], dtype=np.float32)
+    got = angles(np.array([0, 3, -5]), big)
+    assert np.isfinite(got).all() and np.abs(np.hypot(*got.T) - 1).max() <= 2.0 ** -20
