@@ -635,10 +635,10 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) fa_qk_norm_rope_bwd_kernel(
 }
 
 // Adds the partials: q's from rows 0 .. nq-1, k's from rows nq .. n-1.  32
-// columns per CTA, 32 partials at a time.
+// columns per CTA, 32 partials at a time.  The kernel is resident while the partials
+// are still being written, so they are no read-only memory (no __restrict__).
 __global__ void __launch_bounds__(1024)
-    fa_weight_grad_kernel(const float* __restrict__ part, int nq, int n, int d, float* dwq,
-                          float* dwk) {
+    fa_weight_grad_kernel(const float* part, int nq, int n, int d, float* dwq, float* dwk) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float red[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
