@@ -597,10 +597,12 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
 // One CTA per (b, h), thread t owns output column t.  The split weights
 // w_s = 2^(m_s - M) are computed once per split (one thread each) and shared
 // through shared memory; the column sums then read the partials of up to D
-// splits with independent, coalesced loads.
+// splits with independent, coalesced loads.  The kernel is resident while the
+// partials are still being written, so they are no read-only memory (no
+// __restrict__).
 template <int D>
 __global__ void __launch_bounds__(D)
-    fa_decode_combine_kernel(const float* __restrict__ part, const int* __restrict__ seqlens,
+    fa_decode_combine_kernel(const float* part, const int* __restrict__ seqlens,
                              __nv_bfloat16* __restrict__ o, float* __restrict__ lse, int H,
                              int Lmax, int S, int chunk) {
   wait_for_splits();

@@ -26,7 +26,7 @@ def _kernels(text):
 WAITS = r"griddepcontrol\.wait|wait_for_splits\(\)|chain_start\(\)|griddep_wait\(\)"
 
 
-@pytest.mark.parametrize("source", ["fa_rope.cu", "fa_pages.cu", "fa_shared.cu"])
+@pytest.mark.parametrize("source", ["fa_rope.cu", "fa_pages.cu", "fa_shared.cu", "fa_decode.cu"])
 def test_what_an_earlier_kernel_still_writes_is_not_promised_to_be_constant(source):
     """A kernel that starts before the one ahead of it has ended and then waits for it
     must not take that one's results as `const T* __restrict__`, which promises memory
