@@ -162,6 +162,13 @@ Tensor bytes(size_t n, const Tensor& like) {
   return at::empty({static_cast<int64_t>(n)}, like.options().dtype(at::kByte));
 }
 size_t size_of(const Tensor& t) { return static_cast<size_t>(t.nbytes()); }
+// The caller's workspace: as many bytes on the call's device as it says.
+const Tensor& scratch(const Tensor& t, int dev) {
+  if (!t.is_contiguous()) refuse("workspace must be contiguous");
+  if (!t.is_cuda() || t.get_device() != dev)
+    refuse(text("workspace must be on cuda:", dev, ", got ", t.device().str()));
+  return t;
+}
 
 // ---------------------------------------------------------------- rows
 // Element strides (batch, head, token) of [B, H, N, d] or [T, H, d] rows.
@@ -295,7 +302,8 @@ py::tuple qk_norm_rope_bwd(const Tensor& q, const Tensor& k, const Tensor& dq_ou
   row_strides(dk_out, "dk_out", false, strides + 9);
   const Tensor gq = output(dq, q, "dq", dev, strides + 12);
   const Tensor gk = output(dk, k, "dk", dev, strides + 15);
-  Maybe dwq, dwk, ws = workspace;
+  Maybe dwq, dwk, ws;
+  if (workspace) ws = scratch(*workspace, dev);
   const auto f32 = q.options().dtype(at::kFloat);
   if (q_weight) dwq = at::empty({s.d}, f32);
   if (k_weight) dwk = at::empty({s.d}, f32);
@@ -424,7 +432,7 @@ Tensor pages_reserve(const Tensor& block_table, const Tensor& refs, const Tensor
   const OnStream on_stream(stream, dev);
   const Tensor out = granted ? *granted : at::empty({n}, seq_ids.options());
   int* g = ints(out, "granted", n, dev);
-  const Tensor ws = workspace ? *workspace : bytes(api.pages_workspace_size(P, n), refs);
+  const Tensor ws = workspace ? scratch(*workspace, dev) : bytes(api.pages_workspace_size(P, n), refs);
   call("fa_pages_reserve", api.pages_reserve, table.at, table.stride, r, ids, lens, g, table.rows,
        table.cols, P, page_size, n, ws.data_ptr(), size_of(ws), static_cast<fa_stream_t>(on_stream));
   return out;
@@ -443,7 +451,7 @@ Tensor pages_fork(const std::vector<Tensor>& pools, const Tensor& block_table, c
   const OnStream on_stream(stream, dev);
   const Tensor out = made ? *made : at::empty({n}, src.options());
   int* m = ints(out, "made", n, dev);
-  const Tensor ws = workspace ? *workspace : bytes(api.pages_workspace_size(P, n), refs);
+  const Tensor ws = workspace ? scratch(*workspace, dev) : bytes(api.pages_workspace_size(P, n), refs);
   call("fa_pages_fork", api.pages_fork, all.at.data(), all.bytes.data(), all.n, table.at, table.stride,
        lens, r, a, b, m, table.rows, table.cols, P, page_size, n, ws.data_ptr(), size_of(ws),
        static_cast<fa_stream_t>(on_stream));
@@ -473,7 +481,7 @@ Tensor pages_compact(const std::vector<Tensor>& pools, const Tensor& block_table
   const OnStream on_stream(stream, dev);
   const Tensor out = used ? *used : at::empty({1}, refs.options());
   int* u = ints(out, "used", 1, dev);
-  const Tensor ws = workspace ? *workspace : bytes(api.pages_workspace_size(P, 0), refs);
+  const Tensor ws = workspace ? scratch(*workspace, dev) : bytes(api.pages_workspace_size(P, 0), refs);
   call("fa_pages_compact", api.pages_compact, all.at.data(), all.bytes.data(), all.n, table.at,
        table.stride, r, u, table.rows, table.cols, P, ws.data_ptr(), size_of(ws),
        static_cast<fa_stream_t>(on_stream));
@@ -515,7 +523,7 @@ py::tuple decode_shared(const Tensor& q, const Tensor& kpages, const Tensor& vpa
   } else if (want_lse) {
     l = at::empty({B, H}, q.options().dtype(at::kFloat));
   }
-  const Tensor ws = workspace ? *workspace
+  const Tensor ws = workspace ? scratch(*workspace, dev)
                               : bytes(api.decode_shared_workspace_size(B, H, pages.Hkv, prefix.rows, pages.page,
                                                                        prefix.cols, table.cols, d), q);
   call("fa_decode_shared", api.decode_shared, q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
@@ -540,6 +548,7 @@ PYBIND11_MODULE(_fa_native, m) {
   m.def("pages_free", &pages_free);
   m.def("pages_compact", &pages_compact);
   m.def("decode_shared", &decode_shared);
+  m.def("check_workspace", [](const Tensor& t, int dev) { scratch(t, dev); });
   m.def("row_strides", [](const Tensor& t, const char* name, bool written) {
     long long s[3];
     row_strides(t, name, written, s);
