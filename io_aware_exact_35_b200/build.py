@@ -5,8 +5,9 @@
 The library is one CUDA translation unit (csrc/fa_lib.cu) linked against the
 static CUDA runtime; it needs no PyTorch headers.  The output lands in
 io_aware_exact_35_b200/lib/ so that it travels with the source tree.  Beside it
-goes lib/_fa_native.so, the Python binding of the calls that are short on the GPU
-(csrc/fa_binding.cpp, host C++ against PyTorch's headers).
+goes lib/_fa_native.<Python>.torch-<version>.so, the Python binding of the calls that
+are short on the GPU (csrc/fa_binding.cpp, host C++ against PyTorch's headers); its
+name says which Python and PyTorch it is for, so that another one does not load it.
 
 ``--debug`` builds lib/libfa_b200_debug.so with -DFA_DEBUG: the kernels check
 every computed global address and TMA coordinate and record FA_ERR_BOUNDS in
@@ -21,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -29,7 +31,6 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libfa_b200.so")
 DEBUG_LIB = os.path.join(LIBDIR, "libfa_b200_debug.so")
 
-BINDING = os.path.join(LIBDIR, "_fa_native.so")
 BINDING_SOURCES = [os.path.join(CSRC, "fa_binding.cpp"), os.path.join(ROOT, "include", "fa_b200.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -54,17 +55,22 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
-def build_binding(force: bool = False) -> str:
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in BINDING_SOURCES):
-        return BINDING
-    import sysconfig
+def binding_path() -> str:
+    """The native binding of the running Python and PyTorch."""
+    import torch
+    return os.path.join(LIBDIR, f"_fa_native.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 
+
+def build_binding(force: bool = False) -> str:
+    binding = binding_path()
+    if not force and os.path.exists(binding) and all(
+            os.path.getmtime(s) <= os.path.getmtime(binding) for s in BINDING_SOURCES):
+        return binding
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     os.makedirs(LIBDIR, exist_ok=True)
-    tmp = BINDING + ".tmp"
+    tmp = binding + ".tmp"
     # the system's compiler: one that links its C++ runtime in statically gives the
     # process a second one beside PyTorch's
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
@@ -77,9 +83,9 @@ def build_binding(force: bool = False) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("the C++ compiler failed to build _fa_native.so")
-    os.replace(tmp, BINDING)
-    return BINDING
+        raise RuntimeError("the C++ compiler failed to build the native binding")
+    os.replace(tmp, binding)
+    return binding
 
 
 def build(verbose: bool = False, force: bool = False, debug: bool = False) -> str:

@@ -19,6 +19,8 @@ from typing import Optional
 
 import torch
 
+from . import build
+
 # The in-tree build; FA_B200_LIBRARY may point at another build of the same library.
 _LIB_PATH = os.environ.get("FA_B200_LIBRARY") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "lib", "libfa_b200.so")
@@ -424,10 +426,10 @@ _native_module = None
 
 
 def native():
-    """Load _fa_native.so once and hand it the loaded library's entry points."""
+    """Load the native binding once and hand it the loaded library's entry points."""
     global _native_module
     if _native_module is None:
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "_fa_native.so")
+        path = build.binding_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with "
                                "`python -m io_aware_exact_35_b200.build`")
