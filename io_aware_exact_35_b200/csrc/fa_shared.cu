@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* mma_final = p_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+  int* fetched = reinterpret_cast<int*>(smem + L::MISC_OFF + 8);  // ring tiles begun by any producer
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSLOT; ++s) {
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     mbar_init(mma_final, 1);
     *abort_flag = 0;
+    *fetched = 0;
     fence_mbar_init();
   }
   if (warp == WARP_MMA) {
@@ -548,6 +550,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_proxy_async_smem();
       if (ok)
         for (int v = max(0, u - LAG); v < u; ++v) mbar_arrive(&full[v % NSLOT]);
+    } else {
+      // Every copy issued must land before this CTA's shared memory is freed, also
+      // where a wait gave up and no product will ask for it.  Producers that gave up
+      // earlier arrive for the tiles that others began (at most one per slot: to begin
+      // a tile, the one before it in its slot was complete), then each slot's last
+      // tile is waited for.
+      const int most = __reduce_max_sync(0xffffffffu, u);
+      if (lane == 0) atomicMax(fetched, most);
+      named_barrier(1, PRODUCERS);
+      const int all = *static_cast<volatile int*>(fetched);
+      for (; u < all; ++u) mbar_arrive(&full[u % NSLOT]);
+      if (t < NSLOT && t < all) mbar_wait_drain(&full[t], ((all - 1 - t) / NSLOT) & 1);
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));

@@ -40,3 +40,12 @@ def test_what_an_earlier_kernel_still_writes_is_not_promised_to_be_constant(sour
         promised = re.findall(r"const\s+float\d?\s*\*\s*__restrict__\s+(\w+)", parameters)
         assert not promised, f"{name}: {promised}"
     assert seen > 0
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_copies_land_before_their_shared_memory_is_freed(source):
+    """A kernel that fetches by TMA waits for the barriers of its copies on the way
+    out, whether or not the computing warps gave up before they asked for them."""
+    for name, _, body in _kernels(open(os.path.join(CSRC, source)).read()):
+        if re.search(r"tma_load_3d\(|load_rows<", body):
+            assert re.search(r"mbar_wait_drain\(&?\w*full", body), name
