@@ -25,6 +25,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import fa
 
@@ -69,6 +70,7 @@ class _QKNormRope(torch.autograd.Function):
                                interleaved=interleaved)
 
     @staticmethod
+    @once_differentiable  # the kernel's result has no graph: a second derivative is refused
     def backward(ctx, dq_out, dk_out):
         q, k, positions, inv_freq, q_weight, k_weight = ctx.saved_tensors
         dq, dk, dwq, dwk = fa.qk_norm_rope_bwd(q, k, _rows(dq_out), _rows(dk_out), positions,
@@ -83,6 +85,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
                  inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
                  k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
                  interleaved: bool = False):
-    """Differentiable fa.qk_norm_rope (gradients to q, k and the weights)."""
+    """Differentiable fa.qk_norm_rope (gradients to q, k and the weights; second
+    derivatives are refused)."""
     return _QKNormRope.apply(q, k, positions, inv_freq, q_weight, k_weight, float(eps),
                              bool(interleaved))

@@ -59,3 +59,20 @@ def test_frequencies_that_are_no_finite_numbers(fa_mod, cuda_device, d, R, inter
     for a, b in ((oq, rq), (rows, rk)):
         assert torch.isnan(a[..., hit]).all() and torch.equal(a[..., ~hit], b[..., ~hit])
     assert fa_mod.get_device_error() == 0
+
+
+def test_second_derivatives_are_refused(fa_mod, cuda_device):
+    """A loss on the gradients themselves: their graph is not there, and leaving its
+    share out without a word would be a wrong gradient."""
+    from io_aware_exact_35_b200 import autograd
+    g = _gen(3)
+    q, k = (_bf16(g, 20, h, 64).requires_grad_() for h in (4, 2))
+    w = torch.rand(64, generator=g, device=DEV).requires_grad_()
+    pos, inv = torch.arange(20, dtype=torch.int32, device=DEV), _rows.inv_freq(64).to(DEV)
+    oq, ok = autograd.qk_norm_rope(q, k, pos, inv, w, w)
+    first = torch.autograd.grad(oq.float().square().sum() + ok.float().sum(), (q, k, w), create_graph=True)
+    plain = fa_mod.qk_norm_rope_bwd(q.detach(), k.detach(), (2 * oq.detach().float()).bfloat16(), torch.ones_like(k),
+                                    pos, inv, w.detach(), w.detach())
+    assert torch.equal(first[0], plain[0]) and torch.equal(first[1], plain[1])
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (first[0].float().square().sum() + q.float().sum()).backward()
