@@ -539,10 +539,19 @@ fa_status fa_pages_compact(void* const* pools, const size_t* page_bytes, int n_p
  *                 recorded in the device error word; a group behind it begins no
  *                 earlier than the largest end of the groups before it.
  *   block_table : int32 [B, pages_per_seq], row stride table_stride, and
- *   seqlens     : int32 [B], device: each sequence's own pages and length
- *                 (not counting the prefix).
+ *   seqlens     : int32 [B], device: each sequence's own pages and length,
+ *                 both without the prefix: own position 0 is row 0 of the first
+ *                 page listed.  pages_per_seq bounds the own lengths, and
+ *                 the own keys are shared out by it: each warp takes at least
+ *                 1/62 of a full row (up to 1/8 where B * H * d is large), so a
+ *                 table far wider than the lengths leaves the keys to few warps.
+ *                 Pass as many columns as the longest sequence needs (a slice by
+ *                 the strides).
  *   workspace   : fa_decode_shared_workspace_size(...) bytes, 256-byte aligned.
- * A row with no key at all gets O = 0 and LSE = -inf.  Bad page entries are
+ * A row with no key at all gets O = 0 and LSE = -inf.  Scores, softmax states and
+ * sums are held in 32 bits; the probabilities are rounded to bf16 for the product
+ * with V, of the prefix and of the own keys, as in fa_decode_gqa with grouped heads
+ * (fa_decode_paged with Hkv = H holds them in 32 bits).  Bad page entries are
  * treated and reported as in fa_decode_paged.  G = 0, prefix_pages = 0 and
  * pages_per_seq = 0 are allowed.  Returns as fa_decode_paged.
  */

@@ -485,7 +485,8 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kpages: torc
     reads.  Token t goes to place cache_positions[t] (default: positions[t];
     negative: padding, nothing is written) of the sequence in row
     batch_idx[t] (default: t) of block_table.  A token without a page is left
-    out of the cache and reported by get_device_error."""
+    out of the cache and reported by get_device_error.  The rotated keys are in the
+    pages alone; an attention over K and V as tensors takes qk_norm_rope's."""
     return (_native_module or native()).append_paged(
         q, k, v, kpages, vpages, block_table, positions, inv_freq, q_weight, k_weight, batch_idx,
         cache_positions, eps, interleaved, q_out, stream)
@@ -549,8 +550,10 @@ def decode_shared(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor,
     cu_batch[g + 1] - 1 (int32 [G + 1]; None with one group: all), attends the
     first prefix_lens[g] positions of the pages prefix_table[g] [G, pages], read
     once for the group, and then seqlens[b] positions of its own pages
-    block_table[b].  Tables and lengths int32 on the device.  Returns
-    (o [B, H, d], lse [B, H])."""
+    block_table[b], which do not include the prefix's.  Give block_table no more
+    columns than the longest own part needs (a slice of a wider table is fine): the
+    own keys are shared out by its width.  Tables and lengths int32 on the device.
+    Returns (o [B, H, d], lse [B, H])."""
     return (_native_module or native()).decode_shared(
         q, kpages, vpages, prefix_table, prefix_lens, block_table, seqlens, cu_batch, scale, out, lse,
         want_lse, workspace, stream)
