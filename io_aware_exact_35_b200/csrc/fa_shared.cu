@@ -117,40 +117,37 @@ struct Params {
   float scale_log2;
 };
 
-// One warp: first and last batch entry of the groups, 32 at a time in their order
-// (g0 = 0, 32, ..; lane i takes group g0 + i).  A group that leaves the batch or
-// runs backwards is empty and reported.  Each group begins where the one before it
-// ends, so they are disjoint until one is refused; from then on a group begins no
-// earlier than the largest end so far.  An entry therefore has one group, whose CTAs
-// alone write its partials, and there are no more row tiles than the grid has.
-struct GroupRanges {
-  int end = 0;        // the largest end of the groups before g0
-  bool chain = true;  // none of them was refused
+// First and last batch entry of group g; false (and reported, and first = -1) if it
+// leaves the batch or runs backwards.
+__device__ __forceinline__ bool group_range(const int* cu, int B, int g, int& b0, int& b1) {
+  b0 = cu == nullptr ? 0 : cu[g];
+  b1 = cu == nullptr ? B : cu[g + 1];
+  if (b0 >= 0 && b1 >= b0 && b1 <= B) return true;
+  record_error(1 /* FA_ERR_INVALID_ARG */);
+  b0 = b1 = -1;
+  return false;
+}
+
+// Each group begins where the one before it ends, so they are disjoint until one is
+// refused, which is taken as empty; from then on a group begins no earlier than the
+// largest end so far.  An entry therefore has one group, whose CTAs alone write its
+// partials, and there are no more row tiles than the grid has.  A search that meets
+// what it looks for before any refused group needs none of this; the others take the
+// ranges from here, one warp, 32 groups at a time in their order (g0 = 0, 32, ..; lane i
+// takes group g0 + i).
+struct GroupsBehind {
+  int end = 0;  // the largest end of the groups before g0
   __device__ __forceinline__ void take(const int* cu, int B, int G, int g0, int& b0, int& b1) {
-    const int g = g0 + static_cast<int>(threadIdx.x & 31);
-    bool bad = false;
+    const int lane = threadIdx.x & 31;
     b0 = b1 = 0;
-    if (g < G) {
-      b0 = cu == nullptr ? 0 : cu[g];
-      b1 = cu == nullptr ? B : cu[g + 1];
-      bad = b0 < 0 || b1 < b0 || b1 > B;
-      if (bad) {
-        record_error(1 /* FA_ERR_INVALID_ARG */);
-        b0 = b1 = 0;
-      }
-    }
-    const int most = __reduce_max_sync(0xffffffffu, b1);
-    chain = chain && !__any_sync(0xffffffffu, bad);
-    if (!chain) {
-      int upto = b1;  // the largest end up to this lane, then before it
+    if (g0 + lane < G) group_range(cu, B, g0 + lane, b0, b1);
+    int upto = b1;  // the largest end up to this lane, then before it
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1)
-        upto = max(upto, __shfl_up_sync(0xffffffffu, upto, off));
-      const int before = __shfl_up_sync(0xffffffffu, upto, 1);
-      b0 = max(b0, max(end, (threadIdx.x & 31) == 0 ? 0 : before));
-      b1 = max(b0, b1);
-    }
-    end = max(end, most);
+    for (int off = 1; off < 32; off <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, off));
+    const int before = __shfl_up_sync(0xffffffffu, upto, 1);
+    b0 = max(b0, max(end, lane == 0 ? 0 : before));
+    b1 = max(b0, b1);
+    end = max(end, __shfl_sync(0xffffffffu, upto, 31));
   }
 };
 
@@ -238,18 +235,22 @@ __device__ __forceinline__ int choose_splits(const Params& p, const float* sums,
 }
 
 // One warp: the group of the flat tile index, the row tile within it, the
-// group's batch entries and its prefix length.
+// group's batch entries and its prefix length.  BEHIND: a refused group lies before.
+template <bool BEHIND = false>
 __device__ __forceinline__ bool find_tile(const Params& p, int r, int tile, int tile_rows,
                                           int& local, int& g, int& b0, int& b1, int& len) {
+  constexpr int MANY = 1 << 25;  // more tiles than there are; 32 of them are no overflow
   const int lane = threadIdx.x & 31;
   int before = 0;
-  GroupRanges ranges;
+  GroupsBehind ranges;
   for (int g0 = 0; g0 < p.G; g0 += 32) {
-    int n = 0, first, last, length = 0;
-    ranges.take(p.cu, p.B, p.G, g0, first, last);
+    int n = 0, first = 0, last = 0, length = 0;
+    if (BEHIND) ranges.take(p.cu, p.B, p.G, g0, first, last);
     if (g0 + lane < p.G) {
       length = prefix_len(p.lens, g0 + lane, p.pages, p.log2_page);
+      const bool ok = BEHIND || group_range(p.cu, p.B, g0 + lane, first, last);
       n = (static_cast<int>(static_cast<long long>(last - first) * r) + tile_rows - 1) / tile_rows;
+      n = ok ? n : MANY;
     }
     int upto = n;
 #pragma unroll
@@ -260,9 +261,10 @@ __device__ __forceinline__ bool find_tile(const Params& p, int r, int tile, int 
     const unsigned hit = __ballot_sync(0xffffffffu, before + upto > tile);
     if (hit != 0u) {
       const int at = __ffs(hit) - 1;
+      b0 = __shfl_sync(0xffffffffu, first, at);
+      if (!BEHIND && b0 < 0) return find_tile<true>(p, r, tile, tile_rows, local, g, b0, b1, len);
       g = g0 + at;
       local = tile - before - __shfl_sync(0xffffffffu, upto - n, at);
-      b0 = __shfl_sync(0xffffffffu, first, at);
       b1 = __shfl_sync(0xffffffffu, last, at);
       len = __shfl_sync(0xffffffffu, length, at);
       return true;
@@ -270,6 +272,30 @@ __device__ __forceinline__ bool find_tile(const Params& p, int r, int tile, int 
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
   return false;
+}
+
+// One warp: the prefix length of the group that batch entry b belongs to; 0 without
+// one.
+template <bool BEHIND = false>
+__device__ __forceinline__ int entry_prefix(const Params& p, int b) {
+  const int lane = threadIdx.x & 31;
+  GroupsBehind ranges;
+  for (int g0 = 0; g0 < p.G; g0 += 32) {
+    bool mine = false;
+    int len = 0, b0, b1;
+    if (BEHIND) ranges.take(p.cu, p.B, p.G, g0, b0, b1);
+    if (g0 + lane < p.G) {
+      len = prefix_len(p.lens, g0 + lane, p.pages, p.log2_page);
+      if (!BEHIND && !group_range(p.cu, p.B, g0 + lane, b0, b1)) len = -1;
+      mine = (b >= b0 && b < b1) || len < 0;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, mine);
+    if (m != 0u) {
+      len = __shfl_sync(0xffffffffu, len, __ffs(m) - 1);
+      return !BEHIND && len < 0 ? entry_prefix<true>(p, b) : len;
+    }
+  }
+  return 0;
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
@@ -371,6 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
+  int begun = 0;  // ring tiles that this producer has arrived for
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     if (warp == WARP_MMA) {
@@ -485,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) masks[(j % INFO) * 4 + (t >> 5)] = m;
       named_barrier(1, PRODUCERS);
     };
-    int u = 0;
+    int& u = begun;
     auto load = [&](const CUtensorMap& map, const __nv_bfloat16* pool, int j) {
       const int slot = u % NSLOT;
       if (u >= NSLOT && !mbar_wait(&empty[slot], (u / NSLOT - 1) & 1, abort_flag)) return false;
@@ -555,19 +582,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_proxy_async_smem();
       if (ok)
         for (int v = max(0, u - LAG); v < u; ++v) mbar_arrive(&full[v % NSLOT]);
-    } else {
-      // Every copy issued must land before this CTA's shared memory is freed, also
-      // where a wait gave up and no product will ask for it.  Producers that gave up
-      // earlier arrive for the tiles that others began (at most one per slot: to begin
-      // a tile, the one before it in its slot was complete), then each slot's last
-      // tile is waited for.
-      const int most = __reduce_max_sync(0xffffffffu, u);
-      if (lane == 0) atomicMax(fetched, most);
-      named_barrier(1, PRODUCERS);
-      const int all = *static_cast<volatile int*>(fetched);
-      for (; u < all; ++u) mbar_arrive(&full[u % NSLOT]);
-      if (t < NSLOT && t < all) mbar_wait_drain(&full[t], ((all - 1 - t) / NSLOT) & 1);
-      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
@@ -756,6 +770,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
+  }
+  // Every copy issued must land before this CTA's shared memory is freed.  The
+  // products asked for all of them, unless a wait gave up: then producers that gave up
+  // earlier arrive for the tiles that others began (at most one per slot: to begin a
+  // tile, the one before it in its slot was complete), and each slot's last tile is
+  // waited for.  (Row-by-row copies have been waited for by their threads.)
+  if (*abort_flag && p.box > 0) {  // no wait is left that could raise it
+    const bool producer = warp >= 8 && warp < 12;
+    if (producer) atomicMax(fetched, begun);
+    __syncthreads();
+    if (producer) {
+      const int all = *static_cast<volatile int*>(fetched), t = threadIdx.x - 8 * 32;
+      for (; begun < all; ++begun) mbar_arrive(&full[begun % NSLOT]);
+      if (t < NSLOT && t < all) mbar_wait_drain(&full[t], ((all - 1 - t) / NSLOT) & 1);
+    }
   }
   outlast(last);
 }
@@ -1211,22 +1240,7 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32)
     own = p.own_count[static_cast<size_t>(b) * p.Hkv * tiles + h / r * tiles + h % r / 16];
     own_keys = own_len(seqlens, b, Lmax);
   }
-  int group = -1, length = 0;  // the one that b belongs to
-  GroupRanges ranges;
-  for (int g0 = 0; g0 < p.G && group < 0; g0 += 32) {
-    bool mine = false;
-    int len = 0, b0, b1;
-    ranges.take(p.cu, p.B, p.G, g0, b0, b1);
-    if (g0 + lane < p.G) {
-      len = prefix_len(p.lens, g0 + lane, p.pages, p.log2_page);
-      mine = b >= b0 && b < b1;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, mine);
-    if (m != 0u) {
-      group = g0 + __ffs(m) - 1;
-      length = __shfl_sync(0xffffffffu, len, __ffs(m) - 1);
-    }
-  }
+  const int length = entry_prefix(p, b);
   const int nt = (length + KEYS - 1) / KEYS;
   const int np = nt > 0 ? S : 0;
   const int n = np + (own_keys > 0 ? own : 0);  // nothing is written for no keys
