@@ -20,7 +20,7 @@
 // bandwidth.)  A group of lanes keeps one token and walks over its heads, so the
 // rotation and the weight fold into four factors per pair that stay in registers:
 //   out_1 = r (x_1 w_1 cos - x_2 w_2 sin),  out_2 = r (x_2 w_2 cos + x_1 w_1 sin).
-// Angles are formed once per token.  A frequency is held as the fraction of a
+// Angles are formed once per token (fa_angle.h).  A frequency is held as the fraction of a
 // turn per position in 64-bit fixed point, so the product with a position wraps
 // around whole turns by itself and positions of millions lose nothing; the sine
 // and cosine of what is left are 32-bit series.  (With products in double
@@ -35,7 +35,7 @@
 //
 // Measured (three inputs in turn): forward of 8K tokens x 40 heads x 128, 168 MB,
 // 34.3 us a call (31.5 in a graph; a copy of as many bytes 28.4), backward of 16K
-// tokens x 32 heads, 403 MB, 75.6, 8.9K tokens into pages, 218 MB, 40.8.
+// tokens x 32 heads, 403 MB, 75.6 to 76.5, 8.9K tokens into pages, 218 MB, 40.8.
 #include <type_traits>
 
 #include "fa_angle.h"

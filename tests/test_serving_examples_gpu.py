@@ -1,4 +1,4 @@
-"""The README's serving examples do what they say: their text is run."""
+"""The serving examples that users are given do what they say: their text is run."""
 import os
 import re
 
@@ -10,14 +10,14 @@ from tests._parity import check_lse, check_o
 pytestmark = pytest.mark.gpu
 
 DEV = torch.device("cuda:0")
-README = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+GUIDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
 
 
 @pytest.mark.parametrize("prompt_len", [37, 48])
 def test_loop_and_samples_of_one_prompt(fa_mod, cuda_device, prompt_len):
     """A prompt in row 2, samples of it in rows 3 to 6 and another request in row 0:
     steps of the loop, with the shared decode equal to decode_paged over the samples' rows."""
-    with open(README) as f:
+    with open(GUIDE) as f:
         blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
     loop = next(b for b in blocks if "pages_reserve" in b)
     fork, decode = re.split(r"(?=^full = )", next(b for b in blocks if "pages_fork" in b), flags=re.M)
